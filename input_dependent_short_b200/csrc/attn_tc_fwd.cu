@@ -73,24 +73,33 @@ __device__ __forceinline__ uint32_t fma_zero(uint32_t a, uint32_t c) {
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // Adds the value rows that were left out of a diagonal tile's product (a bit of
-// `mask` each) to row r of head h, when the row sees them: o += exp(S - lse) v.
-// Only values with an infinity or a NaN get here, so one more rounding of the
-// finite elements of such a row is no matter.
-__device__ __noinline__ void add_rows(const AttnArgs &a, const Item &t, int h, int r, int row, float lse,
-                                      const volatile uint32_t *mask) {
-    const int hk = h / a.group;
-    const int64_t at = (int64_t)t.start + r;
-    const bf16 *q = static_cast<const bf16 *>(a.q) + at * a.qs + (int64_t)h * a.d;
-    bf16 *o = static_cast<bf16 *>(a.o) + (at * a.Hq + h) * a.d;
-    for (int j = 0; j <= row; ++j) {
+// `mask` each: row j is key key0 + j) to the warp's rows of O in tensor memory,
+// where the row sees them: O += 2^(S c + off) v, in fp32 as the product would,
+// so the finite elements of such rows are as precise as any.  q: this lane's
+// query row; last: the last row of the mask that it sees (-1: none, q is not
+// read).  All lanes of the warp.
+__device__ __noinline__ void add_rows(const AttnArgs &a, uint32_t tO, const bf16 *q, int hk, int64_t key0, int last,
+                                      float c2, float off, const volatile uint32_t *mask) {
+    for (int j = 0; j < ROWS; ++j) {
         if (!((mask[j >> 5] >> (j & 31)) & 1u)) continue;
-        const int64_t key = at - row + j;
-        const bf16 *k = static_cast<const bf16 *>(a.k) + key * a.ks + (int64_t)hk * a.d;
-        const bf16 *v = static_cast<const bf16 *>(a.v) + key * a.vs + (int64_t)hk * a.d;
+        const bf16 *k = static_cast<const bf16 *>(a.k) + (key0 + j) * a.ks + (int64_t)hk * a.d;
+        const bf16 *v = static_cast<const bf16 *>(a.v) + (key0 + j) * a.vs + (int64_t)hk * a.d;
+        const bool sees = j <= last;
         float dot = 0.f;
-        for (int e = 0; e < a.d; ++e) dot = fmaf(__bfloat162float(q[e]), __bfloat162float(k[e]), dot);
-        const float w = exp2f((dot * a.scale - lse) * LOG2E);
-        for (int e = 0; e < a.d; ++e) o[e] = __float2bfloat16_rn(fmaf(w, __bfloat162float(v[e]), __bfloat162float(o[e])));
+        if (sees)
+            for (int e = 0; e < a.d; ++e) dot = fmaf(__bfloat162float(q[e]), __bfloat162float(k[e]), dot);
+        const float w = ex2(fmaf(dot, c2, off));
+        __syncwarp();
+        for (int c = 0; c < a.d; c += 8) {
+            float o[8];
+            tc::tmem_ld8(tO + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (sees) o[e] = fmaf(w, __bfloat162float(v[c + e]), o[e]);
+            tmem_st8(tO + c, o);
+            tmem_wait_st();
+        }
     }
 }
 
@@ -467,7 +476,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool on = r < t.len;
                 if (on) a.lse[h * a.T + at] = lse;
                 const volatile uint32_t *mask = bad + (k % FEED_SLOTS) * 8 + (pair_heads ? 0 : i) * 4;
-                const bool patch = mask[0] | mask[1] | mask[2] | mask[3];
+                if (mask[0] | mask[1] | mask[2] | mask[3])
+                    add_rows(a, tO[i] + lanes, static_cast<const bf16 *>(a.q) + at * a.qs + (int64_t)h * a.d, h / a.group,
+                             at - row, on ? row : -1, c2, -m * c2, mask);
                 bf16 *o = static_cast<bf16 *>(a.o) + (at - lane) * os + (int64_t)h * a.d;  // the warp's first row
                 const int left = t.len - (r - lane);                                       // its rows inside the document
 #pragma unroll 1
@@ -482,7 +493,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(oempty(i));
-                if (patch && on) add_rows(a, t, h, r, row, lse, mask);
             }
             feed.done(k, lane);
         }

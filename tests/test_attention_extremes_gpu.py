@@ -1,0 +1,41 @@
+"""The attention operators where values are not finite or very large, and where
+sizes and offsets leave the ordinary range."""
+
+import math
+
+import pytest
+import torch
+
+import input_dependent_short_b200 as dsc
+from input_dependent_short_b200 import _lib
+
+import attn_ref as ref
+from test_attention_gpu import BF, F32, cu_of, gen, qkv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.fail("needs a CUDA device")
+    yield
+    assert _lib.lib().dsc_check(torch.cuda.current_stream().cuda_stream) == _lib.DSC_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 96])
+def test_an_infinite_channel_leaves_the_others_as_precise(d, dtype):
+    """One element infinite in every value row: infinite in o, while the other
+    elements keep the bound that they have without it."""
+    docs, Hq, Hkv = [300, 50, 128], 4, 2
+    T = sum(docs)
+    q, k, v = (t.clone() for t in qkv(T, Hq, Hkv, d, dtype, seed=120, gain=0.5))
+    scale = 1 / math.sqrt(d)
+    ro, bo, rl, bl = ref.attn_fwd(q, k, v, docs, scale, dtype)
+    v[:, :, 5] = math.inf
+    o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu_of(docs))
+    others = torch.arange(d, device="cuda") != 5
+    assert torch.isposinf(o[:, :, 5]).all()
+    ref.check("o", o[..., others], ro[..., others], bo[..., others])
+    ref.check("lse", lse, rl, bl)
