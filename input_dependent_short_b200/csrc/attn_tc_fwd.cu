@@ -475,10 +475,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float inv = 1.f / l, lse = m * a.scale + logf(l);
                 const bool on = r < t.len;
                 if (on) a.lse[h * a.T + at] = lse;
-                const volatile uint32_t *mask = bad + (k % FEED_SLOTS) * 8 + (pair_heads ? 0 : i) * 4;
-                if (mask[0] | mask[1] | mask[2] | mask[3])
-                    add_rows(a, tO[i] + lanes, static_cast<const bf16 *>(a.q) + at * a.qs + (int64_t)h * a.d, h / a.group,
-                             at - row, on ? row : -1, c2, -m * c2, mask);
+                // The value rows kept out of the products that this tile took part in: its own diagonal's, of which a row
+                // sees those up to itself, and for the second of two tiles of one head also the first one's diagonal, of
+                // which it sees all.
+                const int own = pair_heads ? 0 : i;
+                for (int g = 0; g <= own; ++g) {
+                    const volatile uint32_t *mask = bad + (k % FEED_SLOTS) * 8 + g * 4;
+                    if (mask[0] | mask[1] | mask[2] | mask[3])
+                        add_rows(a, tO[i] + lanes, static_cast<const bf16 *>(a.q) + at * a.qs + (int64_t)h * a.d, h / a.group,
+                                 at - row - (own - g) * ROWS, !on ? -1 : (g < own ? ROWS - 1 : row), c2, -m * c2, mask);
+                }
                 bf16 *o = static_cast<bf16 *>(a.o) + (at - lane) * os + (int64_t)h * a.d;  // the warp's first row
                 const int left = t.len - (r - lane);                                       // its rows inside the document
 #pragma unroll 1

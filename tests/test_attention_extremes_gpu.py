@@ -39,3 +39,33 @@ def test_an_infinite_channel_leaves_the_others_as_precise(d, dtype):
     assert torch.isposinf(o[:, :, 5]).all()
     ref.check("o", o[..., others], ro[..., others], bo[..., others])
     ref.check("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (3, 1), (7, 1), (4, 2)])
+def test_a_bad_value_shows_in_every_row_that_sees_it(Hq, Hkv, dtype):
+    """Odd groups and even ones, in both tiles of 128 that a block may own: a
+    value row with one infinity or NaN shows in that element of all later rows,
+    in no earlier row and no other document, and leaves the other elements their
+    bound."""
+    docs, d = [600, 50], 64
+    T = sum(docs)
+    q, k, v = (t.clone() for t in qkv(T, Hq, Hkv, d, dtype, seed=130, gain=0.5))
+    cu, scale = cu_of(docs), 1 / math.sqrt(d)
+    clean, _ = dsc.dsc_fwd_attn_varlen(q, k, v, cu)
+    ro, bo, rl, bl = ref.attn_fwd(q, k, v, docs, scale, dtype)
+    for at in (0, 40, 127, 128, 200, 255, 256, 300, 511, 599, 610):
+        end = docs[0] if at < docs[0] else T
+        keep = v[at].clone()
+        for x in (math.inf, math.nan):
+            v[at, :, 3] = x
+            o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu)
+            v[at] = keep
+            reached = torch.zeros(T, dtype=torch.bool, device="cuda")
+            reached[at:end] = True
+            assert not torch.isfinite(o[reached, :, 3]).any(), at
+            assert torch.equal(o[~reached], clean[~reached]), at
+            o[reached, :, 3] = clean[reached, :, 3]
+            others = torch.arange(d, device="cuda") != 3
+            ref.check(f"o {at}", o[..., others], ro[..., others], bo[..., others])
+            ref.check("lse", lse, rl, bl)
