@@ -33,6 +33,9 @@
  *    probabilities (and dS in the backward) are rounded to bf16 as operands of
  *    the tensor cores' second product.  DSC_F32: everything fp32.  lse is
  *    always fp32.
+ *  - The weighted values are summed up before the division by the weights' sum,
+ *    no weight above one: the number of keys times the largest |v| must stay
+ *    below fp32's largest number (3.4e38), or the sum becomes infinite.
  *  - Limits: 1 <= T <= 2^30, T * Hq < 2^38, Hq <= 1024, n_docs <= 2^24 and, for
  *    the attention over documents, (T / 32 + n_docs + 2) * Hq < 2^31 - 2^20
  *    (else DSC_ERR_UNSUPPORTED).

@@ -21,9 +21,11 @@
 //   warp 10          looks the diagonal's V tiles over (below)
 //
 // The running maximum is lazy: a row's O and sum are rescaled only when its
-// maximum has risen by a factor of 2^32 of P since its reference was taken.
-// Then P <= 2^32, where bf16, the sum and O (fp32) are as precise as at 1 and
-// far from their largest values.  (With 2^8 the rows that see few keys on the
+// maximum has risen by a factor of 2^16 of P since its reference was taken, and
+// P starts 2^16 below one, so it never exceeds one: O stays below the number of
+// keys times the largest |v|, as in the other kernels.  bf16, the sum and O
+// (fp32) are as precise at 2^-16 as at 1; a weight of less than 2^-110 of its
+// row's largest counts as zero.  (With 2^8 the rows that see few keys on the
 // diagonal rescaled on the next tile nearly always, at 2000 cycles.)  A commit
 // of S(j) also covers the earlier O += P V(j-1), so the softmax may rescale O
 // without a further wait.
@@ -46,6 +48,7 @@ constexpr int THREADS = 384;
 // Registers a thread: launched with 168 (64512 of the SM's 65536), then dealt out per warpgroup: the two
 // softmax warpgroups keep a 128-column row, the third needs few (2 * 128 * 208 + 128 * 80 = 63488).
 constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 80;
+constexpr float HEADROOM = 16.f;  // log2 of the factor by which P may rise before its row is rescaled
 constexpr int SPLIT = 96;  // columns of P after which its first products start
 
 template <int DP> struct Fwd {
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         const int i = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const float c2 = a.scale * LOG2E, slack = 32.f / c2;
+        const float c2 = a.scale * LOG2E, slack = HEADROOM / c2;
         const int64_t os = (int64_t)a.Hq * a.d;
         uint32_t sp = 0, op = 0;
         for (int k = 0;; ++k) {
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int c = 0; c < 32; ++c) top = fmaxf(top, b == quarter && c > lane ? -INFINITY : s[c]);
                     }
                     m = top == -INFINITY ? -1e30f : top;
-                    const u64 off = mk2(-m * c2, -m * c2);
+                    const u64 off = mk2(fmaf(-m, c2, -HEADROOM), fmaf(-m, c2, -HEADROOM));
 #pragma unroll 1
                     for (int b = 0; b < 4; ++b) {
                         if (b <= quarter) {
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tmem_st8(tO[i] + lanes + c, o);
                         }
                     }
-                    const u64 off = mk2(-m * c2, -m * c2);
+                    const u64 off = mk2(fmaf(-m, c2, -HEADROOM), fmaf(-m, c2, -HEADROOM));
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         weights(s + c, off, c);
@@ -465,14 +468,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(pfull(i));
             }
-            if (steps) {  // o = O / l, lse = m scale + log l
+            if (steps) {  // o = O / l, lse = m scale + log(2^16 l)
                 wait(ofull(i), op);
                 op ^= 1u;
                 __syncwarp();
                 tc::fence_after_sync();
                 const int r = t.r0 + (pair_heads ? 0 : i * ROWS) + row, h = pair_heads ? p.h0 + i : p.h0;
                 const int64_t at = (int64_t)t.start + r;
-                const float inv = 1.f / l, lse = m * a.scale + logf(l);
+                const float inv = 1.f / l, lse = m * a.scale + (logf(l) + HEADROOM * LN2);
                 const bool on = r < t.len;
                 if (on) a.lse[h * a.T + at] = lse;
                 // The value rows kept out of the products that this tile took part in: its own diagonal's, of which a row
@@ -483,7 +486,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const volatile uint32_t *mask = bad + (k % FEED_SLOTS) * 8 + g * 4;
                     if (mask[0] | mask[1] | mask[2] | mask[3])
                         add_rows(a, tO[i] + lanes, static_cast<const bf16 *>(a.q) + at * a.qs + (int64_t)h * a.d, h / a.group,
-                                 at - row - (own - g) * ROWS, !on ? -1 : (g < own ? ROWS - 1 : row), c2, -m * c2, mask);
+                                 at - row - (own - g) * ROWS, !on ? -1 : (g < own ? ROWS - 1 : row), c2,
+                                 fmaf(-m, c2, -HEADROOM), mask);
                 }
                 bf16 *o = static_cast<bf16 *>(a.o) + (at - lane) * os + (int64_t)h * a.d;  // the warp's first row
                 const int left = t.len - (r - lane);                                       // its rows inside the document

@@ -69,3 +69,24 @@ def test_a_bad_value_shows_in_every_row_that_sees_it(Hq, Hkv, dtype):
             others = torch.arange(d, device="cuda") != 3
             ref.check(f"o {at}", o[..., others], ro[..., others], bo[..., others])
             ref.check("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (3, 3)])
+@pytest.mark.parametrize("rise", [8, 12, 20, 28])
+def test_large_values_do_not_overflow(rise, Hq, Hkv, dtype):
+    """Values of 2^112 where the first 128 keys weigh 2^rise times as much as the
+    later ones: the weighted sums stay below the number of keys times the values
+    (600 x 2^113 < 2^123), however the running maximum moves."""
+    n, d = 600, 64
+    q = torch.zeros(n, Hq, d, device="cuda")
+    k = torch.zeros(n, Hkv, d, device="cuda")
+    q[:, :, 0] = 1.0
+    k[:, :, 1:] = torch.randn(n, Hkv, d - 1, generator=gen(140), device="cuda")
+    k[:128, :, 0] = rise * math.log(2.0)
+    v = torch.randn(n, Hkv, d, generator=gen(141), device="cuda").clamp(-2, 2) * 2.0 ** 112
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu_of([n]), scale=1.0)
+    ro, bo, rl, bl = ref.attn_fwd(q, k, v, [n], 1.0, dtype)
+    ref.check("o", o, ro, bo)
+    ref.check("lse", lse, rl, bl)
