@@ -19,6 +19,10 @@ constexpr int UNIT = 64;     // tokens of a unit
 constexpr int NTH = 128;     // threads of a block
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
+// The running maximum of a token that counts is at least this, so that it tells
+// "nothing to read" (-infinity: zeros) from scores that are all -infinity (a
+// weights' sum of 0, and 0 / 0 as in the formula).
+constexpr float LOWEST = -3.402823466e38f;
 
 __device__ __forceinline__ int seq_len(const DecodeArgs &a, int b) {
     const int64_t n = a.seq_lens[b], most = a.max_pages * a.page;
@@ -143,8 +147,8 @@ __device__ __forceinline__ void finish_heads(const DecodeArgs &a, const Merge &s
         }
         if (whole) {
             const int64_t r = (int64_t)b * a.Hq + h0 + g0 + g;
-            if (tid < a.d) static_cast<T *>(a.o)[r * a.d + tid] = from_f<T>(ls == 0.f ? 0.f : os / ls);
-            if (tid == 0 && a.lse) a.lse[r] = ls == 0.f ? -INFINITY : (mn + log2f(ls)) * LN2;
+            if (tid < a.d) static_cast<T *>(a.o)[r * a.d + tid] = from_f<T>(mn == -INFINITY ? 0.f : os / ls);
+            if (tid == 0 && a.lse) a.lse[r] = mn == -INFINITY ? -INFINITY : (mn + log2f(ls)) * LN2;
         } else {
             float *p = a.part + ((int64_t)(blockIdx.x * 2 + slot) * GC + g0 + g) * (a.d + 2);
             if (tid < a.d) p[2 + tid] = os;
@@ -241,7 +245,7 @@ template <int GC> __global__ void __launch_bounds__(NTH) k_decode_simt(DecodeArg
             for (int g = 0; g < GC; ++g) {
                 float mn = m[g];
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) mn = fmaxf(mn, s[i][g]);
+                for (int i = 0; i < STEPS; ++i) mn = fmaxf(mn, ok[i] ? fmaxf(s[i][g], LOWEST) : -INFINITY);
                 const float mu = mn == -INFINITY ? 0.f : mn;
                 const float f = exp2f(m[g] - mu);
                 m[g] = mn;
@@ -451,7 +455,7 @@ template <int DP> __global__ void __launch_bounds__(NTH) k_decode_mma(DecodeArgs
             float t = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
             t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 1));
             t = fmaxf(t, __shfl_xor_sync(FULL_MASK, t, 2));
-            const float mn = fmaxf(m[r], t);
+            const float mn = fmaxf(fmaxf(m[r], t), mask ? LOWEST : -INFINITY);
             f[r] = m[r] == mn ? 1.f : exp2f(m[r] - mn);
             moved |= m[r] != mn;
             m[r] = mn;
@@ -565,8 +569,8 @@ template <typename T, int GC> __global__ void __launch_bounds__(128 * JG) k_deco
         os += so[k][col];
     }
     const int64_t r = (int64_t)rec.x * a.Hq + rec.y + g;
-    if (col < a.d) static_cast<T *>(a.o)[r * a.d + col] = from_f<T>(ls == 0.f ? 0.f : os / ls);
-    if (col == 0 && a.lse) a.lse[r] = ls == 0.f ? -INFINITY : (mn + log2f(ls)) * LN2;
+    if (col < a.d) static_cast<T *>(a.o)[r * a.d + col] = from_f<T>(mn == -INFINITY ? 0.f : os / ls);
+    if (col == 0 && a.lse) a.lse[r] = mn == -INFINITY ? -INFINITY : (mn + log2f(ls)) * LN2;
 }
 
 // Four blocks per SM; two where the rings of 128 elements fill the shared memory.

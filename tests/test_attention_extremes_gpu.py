@@ -10,7 +10,7 @@ import input_dependent_short_b200 as dsc
 from input_dependent_short_b200 import _lib
 
 import attn_ref as ref
-from test_attention_gpu import BF, F32, cu_of, gen, qkv
+from test_attention_gpu import BF, F32, cu_of, gen, paged, qkv
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,42 @@ def test_large_values_do_not_overflow(rise, Hq, Hkv, dtype):
     ro, bo, rl, bl = ref.attn_fwd(q, k, v, [n], 1.0, dtype)
     ref.check("o", o, ro, bo)
     ref.check("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 2), (6, 1)])
+def test_scores_that_are_all_minus_infinity(Hq, Hkv, dtype):
+    """Softmax over nothing but -infinity is 0 / 0: NaN, with lse -infinity, in the
+    decode step as in the prompt; zeros are for sequences with nothing to read."""
+    d, lens = 64, [1, 100, 0, 3000]
+    kc, vc, table, sl = paged(lens, 16, Hkv, d, dtype, seed=150)
+    kc[..., 2] = -kc[..., 2].abs() - 1
+    q = torch.randn(4, Hq, d, generator=gen(151), device="cuda").to(dtype)
+    clean = dsc.dsc_decode_attn(q, kc, vc, table, sl)
+    q[:, 0, 2] = math.inf
+    o, lse = dsc.dsc_decode_attn(q, kc, vc, table, sl)
+    some = torch.tensor([0, 1, 3], device="cuda")
+    assert torch.isnan(o[some, 0]).all() and torch.isneginf(lse[:, 0]).all()
+    assert not o[2].any() and torch.isneginf(lse[2]).all()
+    assert torch.equal(o[:, 1:], clean[0][:, 1:]) and torch.equal(lse[:, 1:], clean[1][:, 1:])
+
+    # one key that is finite carries the row, wherever it lies
+    kc[..., 2] = -math.inf
+    for b in (0, 1, 3):
+        pg = int(table[b, (lens[b] // 2) // 16])
+        kc[pg, :, (lens[b] // 2) % 16, 2] = 0.5
+    q[:, :, 2] = 1.0
+    o, lse = dsc.dsc_decode_attn(q, kc, vc, table, sl)
+    assert torch.isfinite(o).all() and torch.isfinite(lse[some]).all()
+    for b in (0, 1, 3):
+        at = lens[b] // 2
+        want = vc[int(table[b, at // 16]), :, at % 16].repeat_interleave(Hq // Hkv, 0)
+        assert torch.equal(o[b], want)          # a weight of one, exactly
+
+    # the prompt
+    x, k, v = (t.clone() for t in qkv(200, Hq, Hkv, d, dtype, seed=152))
+    k[..., 2] = -k[..., 2].abs() - 1
+    x[150, 0, 2] = math.inf
+    o, lse = dsc.dsc_fwd_attn_varlen(x, k, v, cu_of([200]))
+    assert torch.isnan(o[150, 0]).all() and torch.isneginf(lse[0, 150])
+    assert torch.isfinite(o[torch.arange(200, device="cuda") != 150]).all()
