@@ -63,7 +63,7 @@ __device__ __forceinline__ RowInfo row_info(const RopeArgs &a, int64_t t, int la
         if (pos >= 0 && pos < a.max_pages * a.page) {
             const int64_t pg = pos / a.page;
             const int page = a.table[(int64_t)s * a.max_pages + pg];
-            if (page >= 0 && page < a.n_pages) r.slot = (page * a.Hkv * a.page + (pos - pg * a.page)) * (int64_t)a.d;
+            if (page >= 0 && page < a.n_pages) r.slot = ((int64_t)page * a.Hkv * a.page + (pos - pg * a.page)) * a.d;
         }
     }
     return r;

@@ -129,3 +129,39 @@ def test_scores_that_are_all_minus_infinity(Hq, Hkv, dtype):
     o, lse = dsc.dsc_fwd_attn_varlen(x, k, v, cu_of([200]))
     assert torch.isnan(o[150, 0]).all() and torch.isneginf(lse[0, 150])
     assert torch.isfinite(o[torch.arange(200, device="cuda") != 150]).all()
+
+
+def test_append_where_pages_times_heads_pass_2_31():
+    """Pages of one token, so that a page's number times the heads passes 31 bits:
+    every new row lies where the table says and where the decode step reads it."""
+    Hq, Hkv, d, page = 16, 8, 8, 1
+    torch.cuda.empty_cache()
+    n_pages = 2 ** 31 // Hkv + 64               # 34 GB a cache
+    kc, vc = (torch.empty(n_pages, Hkv, page, d, dtype=BF, device="cuda") for _ in range(2))
+    first = n_pages - 48                        # page * heads >= 2^31 from here on
+    assert first * Hkv > 2 ** 31
+    new = [20, 1, 7]
+    order = (first + torch.randperm(40, generator=gen(160), device="cuda")[:28]).to(torch.int32)
+    table = torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+    t0 = 0
+    for s, n in enumerate(new):
+        table[s, :n] = order[t0:t0 + n]
+        t0 += n
+    for c in (kc, vc):
+        c[:64] = 3.0
+        c[first:] = 3.0
+    q, k, v = qkv(28, Hq, Hkv, d, BF, seed=161)
+    sl = torch.tensor(new, dtype=torch.int32, device="cuda")
+    assert dsc.dsc_kv_append(None, k, v, kc, vc, table, sl, cu_seqlens=cu_of(new)) is None
+    at = order.long()
+    assert torch.equal(kc[at, :, 0], k) and torch.equal(vc[at, :, 0], v)
+    rest = torch.ones(n_pages - first, dtype=torch.bool, device="cuda")
+    rest[at - first] = False
+    for c in (kc, vc):
+        assert (c[:64] == 3).all() and (c[first:][rest] == 3).all()
+    o, lse = dsc.dsc_decode_attn(q[:3].contiguous(), kc, vc, table, sl)
+    ro, bo, rl, bl = ref.decode(q[:3], kc, vc, table, new, 1 / math.sqrt(d), BF)
+    ref.check("o", o, ro, bo)
+    ref.check("lse", lse, rl, bl)
+    del kc, vc, c
+    torch.cuda.empty_cache()
