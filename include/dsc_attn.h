@@ -25,7 +25,9 @@
  *    int32 [n_docs + 1] on the device, document i being rows cu_seqlens[i] ..
  *    cu_seqlens[i+1]-1; empty documents are allowed.  Offsets are clamped into
  *    [0, T] and a document that would end before it starts is empty, so a
- *    malformed array gives wrong values, never an access out of bounds.  Rows
+ *    malformed array gives wrong values, never an access out of bounds (the
+ *    attention takes documents that overlap so often that they need more tiles
+ *    than n_docs documents in T rows can have for no documents at all).  Rows
  *    that no document holds (padding behind the last one) are not read; the
  *    outputs' rows there are set to zero, lse to -infinity.
  *  - dtype DSC_BF16: q, k, v, o, dout, dq, dk, dv and the caches are bf16;

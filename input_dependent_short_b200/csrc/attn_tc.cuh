@@ -255,8 +255,7 @@ struct Feed {
         AttnTile t{0, 0, 0, 0};
         int c = -2, total = 0;  // -2: no tile, -1: rows of no document
         if (tid < INLINE_TILES) {
-            const int first = clamp(a.cu[0], 0, T);
-            int last = first;
+            int first = clamp(a.cu[0], 0, T), last = first;
             for (int s = 0; s < a.n_docs; ++s) {
                 const int b = clamp(a.cu[s], 0, T), e = clamp(a.cu[s + 1], b, T), nt = (e - b + rows - 1) / rows;
                 const int j = tid - total;
@@ -266,6 +265,11 @@ struct Feed {
                     c = falling ? nt - 1 - j : j;
                 }
                 total += nt;
+            }
+            if (total > T / rows + a.n_docs + 2) {  // documents that overlap: none at all
+                first = last = T;
+                total = 0;
+                c = -2;
             }
             const int nf = (first + rows - 1) / rows, nb = (T - last + rows - 1) / rows, i = tid - total;
             if (i >= 0 && i < nf + nb) {

@@ -23,11 +23,18 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // values, or queries and gradients.  (23 documents, 16 heads of 128, 268 MB:
 // by cost half of the reads missed L2 and the inputs were read 1.6 times;
 // gradients 359 -> 339 us.  7 documents, 20 MB: 87 us by cost, 92 by document.)
+//
+// Documents that do not overlap have `cap` tiles at most.  Offsets that go back
+// and forth can ask for any number (2^23 documents of 2^30 rows: 2^48 tiles):
+// each warp stops counting once it is above cap, and a total above it counts as
+// no documents at all, so neither the sums nor the time can run away.
 __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__ cu, int n_docs, int T, int rows,
                                                      int shift, int by_doc, int cap, int *__restrict__ rising,
                                                      int *__restrict__ falling_list) {
     __shared__ int hist[NBIN];
     __shared__ int wsum[32];
+    __shared__ long long wtiles[32];
+    __shared__ bool overlap;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool falling = blockIdx.x == 1;
     int *count = falling ? falling_list : rising;
@@ -36,13 +43,16 @@ __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int begin = clampi(cu[0], 0, T);
+    int begin = clampi(cu[0], 0, T);
     int last = begin;  // end of the last document
     for (int pass = 0; pass < 2; ++pass) {
+        long long mine = 0;  // this warp's tiles
         for (int s = warp; s < n_docs; s += 32) {
             const int a = clampi(cu[s], 0, T), b = clampi(cu[s + 1], a, T);
             last = max(last, b);
             const int nt = (b - a + rows - 1) / rows;
+            mine += nt;
+            if (mine > cap) break;
             int first = 0;
             if (by_doc) {
                 if (lane == 0) first = atomicAdd(&hist[min(nt >> shift, NBIN - 1)], nt);
@@ -54,6 +64,7 @@ __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__
                 if (pass && i >= 0 && i < cap) tiles[i] = AttnTile{a, b - a, j * rows, 0};
             }
         }
+        if (pass == 0 && lane == 0) wtiles[warp] = mine;
         __syncthreads();
         if (pass == 0) {  // hist[b] <- tiles in the bins above b
             const int bin = NBIN - 1 - tid;
@@ -72,8 +83,12 @@ __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__
                     if (lane >= o) w += u;
                 }
                 wsum[lane] = w;
+                long long n = wtiles[lane];
+                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(FULL_MASK, n, o);
+                if (lane == 0) overlap = n > cap;
             }
             __syncthreads();
+            if (overlap) break;
             hist[bin] = v - own + (warp ? wsum[warp - 1] : 0);
             __syncthreads();
         }
@@ -83,7 +98,8 @@ __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__
     if (lane == 0) wsum[warp] = last;
     __syncthreads();
     last = __reduce_max_sync(FULL_MASK, wsum[lane]);
-    const int total = hist[0];  // bin 0 is filled last, so its running place is the number of tiles
+    if (overlap) begin = last = T;
+    const int total = overlap ? 0 : hist[0];  // bin 0 is filled last, so its running place is the number of tiles
     const int nf = (begin + rows - 1) / rows, nb = (T - last + rows - 1) / rows;
     for (int i = tid; i < nf + nb; i += 1024) {
         const int s = i < nf ? i * rows : last + (i - nf) * rows, e = i < nf ? begin : T;
@@ -189,7 +205,7 @@ cudaError_t launch_attn_dkv_sum(const Ctx &c, int dtype, const AttnArgs &a) {
 
 // Every document's last tile may be partial; so may the two runs of rows that
 // no document holds.  Offsets that go back and forth can ask for more tiles:
-// those are left out (the list's writes stop at this many).
+// then they count as no documents.
 int64_t attn_max_tiles(int64_t T, int64_t n_docs, int rows) { return T / rows + n_docs + 2; }
 
 size_t attn_list_bytes(int64_t T, int64_t n_docs, int rows) {

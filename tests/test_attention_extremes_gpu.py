@@ -165,3 +165,28 @@ def test_append_where_pages_times_heads_pass_2_31():
     ref.check("lse", lse, rl, bl)
     del kc, vc, c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,times", [(1000, 6), (4096, 30), (2 ** 20, 2 ** 18 + 5)])
+def test_offsets_that_overlap_without_end_count_as_no_documents(T, times, dtype):
+    """0, T, 0, T, ...: up to 2^18 documents of 2^20 rows, whose tiles pass 2^31.
+    Zeros, at once, and nothing outside the outputs is touched.  (Few documents of
+    few rows are a list that the bf16 kernels make themselves.)"""
+    Hq, Hkv, d = 2, 1, 8
+    q, k, v = qkv(T, Hq, Hkv, d, dtype, seed=170)
+    cu = torch.tensor([0, T] * times, dtype=torch.int32, device="cuda")
+    o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu)
+    assert not o.any() and torch.isneginf(lse).all()
+    guard = torch.full((T + 2, (Hq + 2 * Hkv) * d), 7.0, dtype=dtype, device="cuda")
+    h = guard[1:-1].unflatten(1, (Hq + 2 * Hkv, d))
+    out = h[:, :Hq], h[:, Hq:Hq + Hkv], h[:, Hq + Hkv:]
+    for g in dsc.dsc_bwd_attn_varlen(q, k, v, o, lse, o, cu, out=out):
+        assert not g.any()
+    assert (guard[0] == 7).all() and (guard[-1] == 7).all()
+    # and the next call, with documents, is as ever
+    n = min(T, 700)
+    cu = cu_of([n // 3, n - n // 3])
+    o, lse = dsc.dsc_fwd_attn_varlen(q[:n], k[:n], v[:n], cu)
+    ro, bo, rl, bl = ref.attn_fwd(q[:n], k[:n], v[:n], [n // 3, n - n // 3], 1 / math.sqrt(d), dtype)
+    ref.check("o", o, ro, bo)
