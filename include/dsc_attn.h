@@ -112,6 +112,12 @@ DSC_API dsc_status dsc_bwd_attn_varlen(const dsc_attn_problem *p, const int32_t 
                                        void *dv, int64_t dv_stride, void *workspace, size_t workspace_bytes,
                                        void *stream);
 
+/* Failure-detection self-test of the tensor-core kernels' hand-over of work, as
+ * dsc_selftest_timeout: one small kernel whose waits for an item run out (limit
+ * about 5 ms).  No item is taken, and the next dsc_check() on the stream
+ * returns DSC_ERR_TIMEOUT and clears it (DSC_ERR_CUDA if one was taken). */
+DSC_API dsc_status dsc_selftest_attn_timeout(void *stream);
+
 /* -------------------------------------------------------------- rotation ---
  * Row t of a document at place m (0 for its first row): each pair (a, b) of a
  * head becomes (a cos x - b sin x, a sin x + b cos x), x = m * inv_freq[i],

@@ -89,6 +89,7 @@ _SIGS = {
     "dsc_bwd_attn_varlen_workspace_bytes": (C.c_size_t, [_PA, C.c_int64]),
     "dsc_bwd_attn_varlen": (C.c_int, [_PA, _v, C.c_int64, _v, _v, _v, _v, _v, _v, _v, C.c_int64, _v, C.c_int64, _v,
                                       C.c_int64, _v, C.c_size_t, _v]),
+    "dsc_selftest_attn_timeout": (C.c_int, [_v]),
     "dsc_fwd_rope_varlen": (C.c_int, [_PR, _v, C.c_int64, _v, _v, _v, _v, _v, _v]),
     "dsc_bwd_rope_varlen": (C.c_int, [_PR, _v, C.c_int64, _v, _v, _v, _v, _v, _v]),
     "dsc_kv_append": (C.c_int, [_PR, _PC, _v, C.c_int64, _v, _v, _v, _v, _v, _v, _v, _v, _v, _v, _v]),

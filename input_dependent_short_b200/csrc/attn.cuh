@@ -91,6 +91,7 @@ cudaError_t launch_attn_dkv_simt(const Ctx &c, const AttnArgs &a, int64_t max_ti
 int attn_fwd_tc_rows(int group);
 cudaError_t launch_attn_fwd_tc(const Ctx &c, const AttnArgs &a, int64_t max_tiles);
 int take_attn_fwd_status(cudaStream_t stream);
+cudaError_t launch_feed_selftest(cudaStream_t stream);
 
 // attn_tc_bwd.cu: the tensor-core gradients (bf16); tiles of ATTN_TC_BWD_ROWS rows
 constexpr int ATTN_TC_BWD_ROWS = 128;

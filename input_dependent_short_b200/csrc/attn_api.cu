@@ -241,6 +241,8 @@ dsc_status dsc_bwd_attn_varlen(const dsc_attn_problem *p, const int32_t *cu_seql
     return done(e);
 }
 
+dsc_status dsc_selftest_attn_timeout(void *stream) { return done(launch_feed_selftest(static_cast<cudaStream_t>(stream))); }
+
 dsc_status dsc_fwd_rope_varlen(const dsc_rope_problem *p, const int32_t *cu_seqlens, int64_t n_docs, const void *q,
                                const void *k, const float *inv_freq, void *q_out, void *k_out, void *stream) {
     return rope(p, cu_seqlens, n_docs, q, k, inv_freq, q_out, k_out, 1.f, stream);

@@ -220,7 +220,10 @@ __device__ __forceinline__ bool any_nonfinite(const uint4 &x) {
 // until none is left, so the barriers, tensor memory and instruction cache are
 // set up once and an item's loads and first products run under the previous
 // one's epilogue.  The loading lane draws the items and passes them on through
-// FEED_SLOTS slots of shared memory, each read by `readers` warps.
+// FEED_SLOTS slots of shared memory, each read by `readers` warps.  A wait that
+// runs out ends the feed for its warp: a slot that was not seen full, or not
+// seen empty, is neither read nor written, so no warp works on an item that
+// was never there.
 constexpr int FEED_SLOTS = 4;
 
 struct Item {
@@ -291,7 +294,8 @@ struct Feed {
     }
     // The loading lane: this block's item k.  Items of a list in memory are drawn from its counter (the first is the
     // block's index), those of a short list dealt out in turn.
-    template <typename Wait> __device__ Item draw(int k, const AttnArgs &a, int heads, Wait &&wait) const {
+    template <typename Wait>
+    __device__ Item draw(int k, const AttnArgs &a, int heads, Wait &&wait, const bool &timed_out) const {
         const int i = k == 0 || a.cu ? (int)(blockIdx.x + k * gridDim.x) : (int)gridDim.x + atomicAdd(a.list.next, 1);
         const int tile = i / heads;
         Item it{0, 0, 0, -1};
@@ -300,12 +304,16 @@ struct Feed {
             it = Item{t.start, t.len, t.r0, i % heads};
         }
         if (k >= FEED_SLOTS) wait(empty(k), (uint32_t)((k / FEED_SLOTS - 1) & 1));
+        if (timed_out) return Item{0, 0, 0, -1};
         items[k % FEED_SLOTS] = it;
         tc::mbar_arrive(full(k));
         return it;
     }
-    template <typename Wait> __device__ Item get(int k, Wait &&wait) const {
+    // All lanes of a reading warp, which all end the feed when the wait of one has run out.
+    template <typename Wait> __device__ Item get(int k, Wait &&wait, bool &timed_out) const {
         wait(full(k), (uint32_t)((k / FEED_SLOTS) & 1));
+        timed_out = __any_sync(FULL_MASK, timed_out);
+        if (timed_out) return Item{0, 0, 0, -1};
         const Item it = items[k % FEED_SLOTS];
         __syncwarp();
         return it;

@@ -229,17 +229,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             int g = 0, uses = 0;  // steps and items so far
             for (int k = 0;; ++k) {
-                const Item t = feed.draw(k, a, heads, wait);
+                const Item t = feed.draw(k, a, heads, wait, timed_out);
                 if (t.h < 0) break;
                 if (t.len < 0) continue;
                 const Plan p = plan(t);
                 if (uses) wait(kvempty, (uint32_t)((uses - 1) & 1));
+                if (timed_out) break;
                 ++uses;
                 tc::mbar_expect_tx(kvfull, 2 * S::TILE);
                 load_rows<DP>(sbase, &maps.k, p.hk, p.row0, kvfull);
                 load_rows<DP>(sbase + S::TILE, &maps.v, p.hk, p.row0, kvfull);
                 for (int u = 0; u < p.N; ++u, ++g) {
                     if (g >= S::STAGES) wait(empty(g), (uint32_t)((g / S::STAGES - 1) & 1));
+                    if (timed_out) break;
                     const uint32_t bar = p.partial(u) ? raw(g) : full(g);
                     const int h = p.h0 + u / p.nqt, r = p.row0 + (u % p.nqt) * ROWS;
                     tc::mbar_expect_tx(bar, 2 * S::TILE);
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 9) {
         int g0 = 0, uses = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int g = 0;
         uint32_t rp = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float c2 = a.scale * LOG2E;
         int g = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             const Plan p = plan(t);
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int uses = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
@@ -557,13 +559,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == 8) {
         if (lane == 0) {
-            int g = 0, uses = 0;  // steps and items so far
+            int g = 0, gk = 0, uses = 0;  // steps, K tiles loaded and items so far
             for (int k = 0;; ++k) {
-                const Item t = feed.draw(k, a, heads, wait);
+                const Item t = feed.draw(k, a, heads, wait, timed_out);
                 if (t.h < 0) break;
                 if (t.len < 0) continue;
                 const int N = steps(t), rows = rows_of(t), hk = t.h / a.group;
                 if (uses) wait(qempty, (uint32_t)((uses - 1) & 1));
+                if (timed_out) break;
                 ++uses;
                 tc::mbar_expect_tx(qfull, 2 * S::TILE);
                 load_rows<DP>(sbase, &maps.q, t.h, t.start + t.r0, qfull);
@@ -571,18 +574,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < N; ++j, ++g) {
                     const int r = t.start + (N - 1 - j) * ROWS, sk = g % S::KS, sv = g % S::VS;
                     if (g >= S::KS) wait(kempty(sk), (uint32_t)((g / S::KS - 1) & 1));
+                    if (timed_out) break;
                     const uint32_t bar = j == 0 && rows < ROWS ? kraw(sk) : kfull(sk);
                     tc::mbar_expect_tx(bar, S::TILE);
                     load_rows<DP>(kslot(g), &maps.k, hk, r, bar);
+                    gk = g + 1;
                     if (g >= S::VS) wait(vempty(sv), (uint32_t)((g / S::VS - 1) & 1));
+                    if (timed_out) break;
                     tc::mbar_expect_tx(vfull(sv), S::TILE);
                     load_rows<DP>(vslot(g), &maps.v, hk, r, vfull(sv));
                 }
             }
             // every load has landed before the block may end
             if (uses) tc::mbar_wait(qfull, (uint32_t)((uses - 1) & 1), limit);
-            for (int s = 0; s < S::KS && s < g; ++s) {
-                const int last = s + ((g - 1 - s) / S::KS) * S::KS;
+            for (int s = 0; s < S::KS && s < gk; ++s) {
+                const int last = s + ((gk - 1 - s) / S::KS) * S::KS;
                 tc::mbar_wait(kfull(s), (uint32_t)((last / S::KS) & 1), limit);
             }
             for (int s = 0; s < S::VS && s < g; ++s) {
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 9) {
         int g0 = 0, uses = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
@@ -638,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int g = 0;
         uint32_t rp = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float c2 = a.scale * LOG2E;
         int g = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             bf16 *dq = static_cast<bf16 *>(a.dq) + (int64_t)t.h * a.d;
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int uses = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;

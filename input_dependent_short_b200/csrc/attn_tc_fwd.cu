@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) {
                 int u = 0, uses[2] = {0, 0};  // ring tiles and query tiles loaded so far
                 for (int k = 0;; ++k) {
-                    const Item t = feed.draw(k, a, heads, wait);
+                    const Item t = feed.draw(k, a, heads, wait, timed_out);
                     if (t.h < 0) break;
                     if (t.len < 0) continue;
                     const Plan p = plan(t);
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 2; ++i)
                         if (p.n[i]) {
                             if (uses[i]) wait(qempty(i), (uint32_t)((uses[i] - 1) & 1));
+                            if (timed_out) break;
                             ++uses[i];
                             tc::mbar_expect_tx(qfull(i), S::TILE);
                             load_rows<DP>(sbase + i * S::TILE, &maps.q, pair_heads ? p.h0 + i : p.h0,
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int v = 0; v < 2 * p.J; ++v, ++u) {  // K, V of each step in turn
                         const int s = u % S::SLOTS, it = v >> 1;
                         if (u >= S::SLOTS) wait(empty(s), (uint32_t)((u / S::SLOTS - 1) & 1));
+                        if (timed_out) break;
                         const uint32_t bar = (v & 1) && p.diag(it) >= 0 ? raw(s) : full(s);
                         tc::mbar_expect_tx(bar, S::TILE);
                         load_rows<DP>(sbase + S::RING + s * S::TILE, v & 1 ? &maps.v : &maps.k, hk,
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_after_sync();
             };
             for (int k = 0;; ++k) {
-                const Item t = feed.get(k, wait);
+                const Item t = feed.get(k, wait, timed_out);
                 feed.done(k, lane);
                 if (t.h < 0) break;
                 if (t.len < 0) continue;
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int u0 = 0;
             uint32_t rp = 0;  // a bit per slot: parity of its raw barrier
             for (int k = 0;; ++k) {
-                const Item t = feed.get(k, wait);
+                const Item t = feed.get(k, wait, timed_out);
                 if (t.h < 0) break;
                 if (t.len < 0) {
                     feed.done(k, lane);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t os = (int64_t)a.Hq * a.d;
         uint32_t sp = 0, op = 0;
         for (int k = 0;; ++k) {
-            const Item t = feed.get(k, wait);
+            const Item t = feed.get(k, wait, timed_out);
             if (t.h < 0) break;
             const Plan p = plan(t);
             if (t.len < 0) {  // rows that no document holds
@@ -519,6 +521,38 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+// A feed whose waits run out: warp 1 reads item 0, which nothing puts there, and
+// warp 0 draws an item for a slot that nothing empties.  Both must end the feed,
+// and the slot keeps what it held; anything else is reported as an error of its
+// own.
+__global__ void k_feed_selftest(long long limit) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Feed feed(tc::smem_u32(smem), smem, 0);
+    int32_t cu[2] = {0, 0};
+    AttnArgs a{};
+    a.cu = cu;  // a list made here; its documents are not read
+    if (tid == 0) {
+        feed.init(1);
+        for (int i = 0; i < FEED_SLOTS; ++i) feed.items[i] = Item{1 << 29, 1 << 29, 0, 7};
+        *feed.head = INLINE_TILES;
+        for (int i = 0; i < INLINE_TILES; ++i) feed.tiles()[i] = AttnTile{0, 1, 0, 0};
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    bool timed_out = false;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!timed_out && !tc::mbar_wait(bar, parity, limit)) timed_out = true;
+    };
+    int h = -1;
+    if (warp == 1) h = feed.get(0, wait, timed_out).h;
+    else if (lane == 0) h = feed.draw(FEED_SLOTS, a, 1, wait, timed_out).h;
+    const bool part = tid == 0 || warp == 1, ok = h < 0 && timed_out && feed.items[0].h == 7;
+    if (part && ok) atomicExch(&g_dsc_status_attn_fwd, (int)DSC_ERR_TIMEOUT);
+    __syncthreads();
+    if (part && !ok) atomicExch(&g_dsc_status_attn_fwd, (int)DSC_ERR_CUDA);
+}
+
 template <int DP> cudaError_t launch(const Ctx &c, const AttnArgs &a, int64_t max_tiles) {
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(k_attn_fwd_tc<DP>, Fwd<DP>::TOTAL, ready);
@@ -551,5 +585,11 @@ cudaError_t launch_attn_fwd_tc(const Ctx &c, const AttnArgs &a, int64_t max_tile
 }
 
 int take_attn_fwd_status(cudaStream_t stream) { return attn_tc::take(stream); }
+
+cudaError_t launch_feed_selftest(cudaStream_t stream) {
+    attn_tc::k_feed_selftest<<<1, 64, attn_tc::Feed::BYTES, stream>>>(10000000ll);
+    count_launch();
+    return cudaGetLastError();
+}
 
 }  // namespace dsc

@@ -190,3 +190,21 @@ def test_offsets_that_overlap_without_end_count_as_no_documents(T, times, dtype)
     o, lse = dsc.dsc_fwd_attn_varlen(q[:n], k[:n], v[:n], cu)
     ro, bo, rl, bl = ref.attn_fwd(q[:n], k[:n], v[:n], [n // 3, n - n // 3], 1 / math.sqrt(d), dtype)
     ref.check("o", o, ro, bo)
+
+
+def test_a_feed_whose_waits_run_out_hands_over_no_item():
+    """The kernels' work feed with a wait that nothing ends (a few milliseconds):
+    the reader and the drawing lane both stop, the time-out reaches the host and
+    is cleared, and the next call is right."""
+    L, s = _lib.lib(), torch.cuda.current_stream().cuda_stream
+    assert L.dsc_check(s) == _lib.DSC_OK
+    n0 = L.dsc_launch_count()
+    assert L.dsc_selftest_attn_timeout(s) == _lib.DSC_OK
+    assert L.dsc_launch_count() == n0 + 1
+    assert L.dsc_check(s) == _lib.DSC_ERR_TIMEOUT
+    assert L.dsc_check(s) == _lib.DSC_OK
+    docs = [300, 77]
+    q, k, v = qkv(377, 4, 2, 64, BF, seed=180)
+    o, _ = dsc.dsc_fwd_attn_varlen(q, k, v, cu_of(docs))
+    ro, bo, _, _ = ref.attn_fwd(q, k, v, docs, 0.125, BF)
+    ref.check("o", o, ro, bo)
