@@ -99,8 +99,7 @@ DSC_API dsc_status dsc_fwd_attn_varlen(const dsc_attn_problem *p, const int32_t 
  * dq [T, Hq, d], dk and dv [T, Hkv, d] with rows dq_stride, dk_stride and
  * dv_stride elements apart (they may be views of one gradient of a packed
  * projection; the elements between rows are not touched).  With DSC_BF16, D
- * comes from the rounded o only for the dq of rows behind a document's first
- * 128; elsewhere it is summed up from P in fp32; a row that is not
+ * is summed up from P in fp32 and o is not read; a row that is not
  * finite may also show in the rows of its own tile of 128 that it does not reach
  * by the formula (a masked pair's zero is multiplied with it); with DSC_F32 and
  * in the forward it does not.  Deterministic: no sum depends on the order in

@@ -73,9 +73,8 @@ size_t attn_list_bytes(int64_t T, int64_t n_docs, int rows);
 // `falling` may be null: one list only.
 cudaError_t launch_attn_tiles(const Ctx &c, const int32_t *cu, int64_t n_docs, int64_t T, int rows, size_t bytes,
                               void *rising, void *falling);
-// delta[h][t] = dout[t][h] . o[t][h]
-cudaError_t launch_attn_delta(const Ctx &c, int dtype, int64_t T, int Hq, int d, const void *o, const void *dout,
-                              float *delta);
+// delta[h][t] = dout[t][h] . o[t][h] (fp32; with bf16 the dq kernel forms it from the probabilities)
+cudaError_t launch_attn_delta(const Ctx &c, int64_t T, int Hq, int d, const float *o, const float *dout, float *delta);
 
 // Blocks that share a key tile's (of `rows` keys) group of query heads, and the sum of their parts.
 int attn_dkv_splits(int64_t T, int rows, int Hkv, int group, int sms);

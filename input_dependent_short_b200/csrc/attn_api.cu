@@ -225,14 +225,16 @@ dsc_status dsc_bwd_attn_varlen(const dsc_attn_problem *p, const int32_t *cu_seql
         a.cu = cu_seqlens;
         a.n_docs = (int)n_docs;
     }
-    if (e == cudaSuccess) e = launch_attn_delta(c, p->dtype, p->T, a.Hq, a.d, o, dout, delta);
     const TileList rising = list_at(w), falling = list_at(w + lb);
-    if (bf) {  // dq first: it makes delta exact
+    if (bf) {  // dq first: it makes delta, from the probabilities
         a.list = rising;
         if (e == cudaSuccess) e = launch_attn_dq_tc(c, a, tiles);
         a.list = falling;
         if (e == cudaSuccess) e = launch_attn_dkv_tc(c, a, tiles);
-    } else {  // the longer kernel first: the other's blocks fill its last SMs (187 us against 197, 1500 tokens)
+    } else {
+        if (e == cudaSuccess)
+            e = launch_attn_delta(c, p->T, a.Hq, a.d, static_cast<const float *>(o), static_cast<const float *>(dout), delta);
+        // the longer kernel first: the other's blocks fill its last SMs (187 us against 197, 1500 tokens)
         a.list = falling;
         if (e == cudaSuccess) e = launch_attn_dkv_simt(c, a, tiles);
         a.list = rising;

@@ -14,13 +14,17 @@
 // alternative, adding dq up in memory from the first, needs 32-bit atomics
 // whose order would change the result.
 //
-// D_i = dout_i . o_i comes from the o that the caller has, rounded to bf16, and
-// its error (2^-9 |dout| |o|) can be as large as what remains of dP - D where
-// few keys carry a row.  Since sum_j P_ij = 1, the error is sum_j dS_ij, so the
-// dq kernel, which runs first, sums dS up in fp32 and leaves the right D for the
-// dk, dv kernel; a row whose keys are all in one tile (documents up to 128
-// rows, and every document's first 128) has D = sum_j P_ij dP_ij before its dS
-// is formed.
+// D_i = dout_i . o_i = sum_j P_ij dP_ij is summed up from P and dP in fp32, by the
+// dq kernel, which runs first and leaves it to the other.  (From the o that the
+// caller has, rounded to bf16, it would be off by 2^-9 |dout| |o|, which can be
+// all that remains of dP - D where few keys carry a row: dq was then 1.5 to 1.9
+// times as far off as the products' own roundings leave it.)  An item of N key
+// tiles takes 2 N - 1 steps: the sums over the tiles before the diagonal, the
+// diagonal's sum and at once its gradient, and the gradient of the others from
+// there back.  5 products a pair of tiles instead of 3, and no pass over o: the
+// gradients of 16384 tokens in 23 documents, 16 heads of 128, take 299 us
+// against 283 with a D from o, of one document of 8192, 32/8 heads, 1887
+// against 1471 (the added steps' K and V come from L2 at 10 TB/s, which bounds them).
 //
 // Roles as in the forward: warps 0-7 do the elementwise part (a thread owns a
 // row of the 128 x 128 tile and 64 of its columns; P^T and dS^T go back to
@@ -36,7 +40,7 @@
 // warps do (step u of dk/dv):   ... | dv(u), S(u+1) | dk(u), dP(u+1) | ...
 //                                     | dS(u) formed | P(u+1) formed  |
 // (heads of 64: S(u+2), into the second of two buffers, in the place of S(u+1))
-// and of dq, with two S buffers: ... | dP(j+1), dq(j), S(j+2) | ...
+// and of dq, with two S buffers: ... | dP(j+1), dq(j), S(j+2) | ... (dq(j) from the diagonal on)
 #include "attn_tc.cuh"
 
 namespace dsc {
@@ -551,8 +555,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     auto kslot = [&](int g) { return sbase + S::KRING + (uint32_t)(g % S::KS) * S::TILE; };
     auto vslot = [&](int g) { return sbase + S::VRING + (uint32_t)(g % S::VS) * S::TILE; };
-    // An item: N key tiles, from the diagonal down; `rows` rows of the query tile, and keys of the first key tile.
-    auto steps = [](const Item &t) { return t.r0 / ROWS + 1; };
+    // An item: N key tiles in 2 N - 1 steps, up to the diagonal (step N - 1) and back; `rows` rows of the query tile, and
+    // keys of the diagonal's tile.
+    auto tiles = [](const Item &t) { return t.r0 / ROWS + 1; };
     auto rows_of = [](const Item &t) { return min(ROWS, t.len - t.r0); };
 
     if (warp >= 8 && warp < 12) {
@@ -564,18 +569,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const Item t = feed.draw(k, a, heads, wait, timed_out);
                 if (t.h < 0) break;
                 if (t.len < 0) continue;
-                const int N = steps(t), rows = rows_of(t), hk = t.h / a.group;
+                const int N = tiles(t), rows = rows_of(t), hk = t.h / a.group;
                 if (uses) wait(qempty, (uint32_t)((uses - 1) & 1));
                 if (timed_out) break;
                 ++uses;
                 tc::mbar_expect_tx(qfull, 2 * S::TILE);
                 load_rows<DP>(sbase, &maps.q, t.h, t.start + t.r0, qfull);
                 load_rows<DP>(sbase + S::TILE, &maps.dout, t.h, t.start + t.r0, qfull);
-                for (int j = 0; j < N; ++j, ++g) {
-                    const int r = t.start + (N - 1 - j) * ROWS, sk = g % S::KS, sv = g % S::VS;
+                for (int j = 0; j < 2 * N - 1; ++j, ++g) {
+                    const int r = t.start + (j < N ? j : 2 * N - 2 - j) * ROWS, sk = g % S::KS, sv = g % S::VS;
                     if (g >= S::KS) wait(kempty(sk), (uint32_t)((g / S::KS - 1) & 1));
                     if (timed_out) break;
-                    const uint32_t bar = j == 0 && rows < ROWS ? kraw(sk) : kfull(sk);
+                    const uint32_t bar = j == N - 1 && rows < ROWS ? kraw(sk) : kfull(sk);
                     tc::mbar_expect_tx(bar, S::TILE);
                     load_rows<DP>(kslot(g), &maps.k, hk, r, bar);
                     gk = g + 1;
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
-            const int N = steps(t);
+            const int first = tiles(t) - 1, M = 2 * first + 1;  // the first step with a gradient, steps
             auto scores = [&](int g) {
                 wait(kfull(g % S::KS), (uint32_t)((g / S::KS) & 1));
                 tc::fence_after_sync();
@@ -620,23 +625,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait(qfull, (uint32_t)(uses & 1));
             scores(g0);
             weights(g0);
-            if (N > 1) scores(g0 + 1);
+            if (M > 1) scores(g0 + 1);
             else commit(qempty);
-            for (int j = 0; j < N; ++j) {
+            for (int j = 0; j < M; ++j) {
                 const int g = g0 + j;
                 wait(dsfull, (uint32_t)(g & 1));
                 tc::fence_after_sync();
-                if (j + 1 < N) {
+                if (j + 1 < M) {
                     weights(g + 1);
-                    if (j + 2 == N) commit(qempty);  // its scores were issued a step ago
+                    if (j + 2 == M) commit(qempty);  // its scores were issued a step ago
                 }
-                if (j == 0 && uses) wait(accempty, (uint32_t)((uses - 1) & 1));
-                mma_rows<DP, 0, ROWS / 16, true>(tQ, tS + 128u * (g & 1), kslot(g), j > 0);
+                if (j == first && uses) wait(accempty, (uint32_t)((uses - 1) & 1));
+                if (j >= first) mma_rows<DP, 0, ROWS / 16, true>(tQ, tS + 128u * (g & 1), kslot(g), j > first);
                 commit(kempty(g % S::KS));
-                if (j + 2 < N) scores(g + 2);
+                if (j + 2 < M) scores(g + 2);
             }
             commit(accfull);
-            g0 += N;
+            g0 += M;
             ++uses;
         }
         if (uses) tc::mbar_wait(accfull, (uint32_t)((uses - 1) & 1), limit);  // every product is done
@@ -648,16 +653,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             feed.done(k, lane);
             if (t.h < 0) break;
             if (t.len < 0) continue;
-            const int rows = rows_of(t), s = g % S::KS;
+            const int rows = rows_of(t), first = tiles(t) - 1, s = (g + first) % S::KS;
             if (rows < ROWS) {
                 wait(kraw(s), (rp >> s) & 1u);
                 rp ^= 1u << s;
-                zero_tail<DP>(smem + (kslot(g) - sbase), rows, lane);
+                zero_tail<DP>(smem + (kslot(g + first) - sbase), rows, lane);
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(kfull(s));
             }
-            g += steps(t);
+            g += 2 * first + 1;
         }
     }
     } else if (warp < 8) {
@@ -675,12 +680,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 zero_head(dq + t.start * a.dqs, a.dqs, -t.len, a.d, tid);
                 continue;
             }
-            const int N = steps(t);
+            const int first = tiles(t) - 1, M = 2 * first + 1;
             const int64_t r = (int64_t)t.start + t.r0 + row;
             const bool on = row < rows_of(t);
             const float nl = on ? -a.lse[t.h * a.T + r] * LOG2E : -INFINITY;
-            float nd = on ? -a.delta[t.h * a.T + r] : 0.f;
-            u64 off = 0;  // sum of dS
+            float nd = 0.f;  // -D
+            u64 sum[2] = {0, 0};  // of P dP, this half's columns
             // Sum over the row of both halves' `own`.
             auto row_total = [&](float own) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");  // the last item's have been read
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 return sums[row] + sums[ROWS + row];
             };
-            for (int j = 0; j < N; ++j, ++g) {
+            for (int j = 0; j < M; ++j, ++g) {
                 const uint32_t tb = tS + 128u * (g & 1) + lanes + c0;
                 float w[64];
                 wait(sfull(g & 1), (uint32_t)((g >> 1) & 1));
@@ -703,17 +708,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                 wait(dpfull, (uint32_t)(g & 1));
                 __syncwarp();
                 tc::fence_after_sync();
-                if (N == 1) {  // all of the row's pairs are here: D itself
-                    float own = 0.f;
-#pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        float x[32];
-                        tmem_ld32(tP + lanes + c0 + 32 * e, x);
-                        tc::tmem_wait_ld();
+                if (j <= first) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) own += c0 + 32 * e + c > row ? 0.f : (e ? w[32 + c] : w[c]) * x[c];
+                    for (int e = 0; e < 64; e += 32) {
+                        float x[32];
+                        tmem_ld32(tP + lanes + c0 + e, x);
+                        tc::tmem_wait_ld();
+                        if (j == first) {  // a masked pair counts for nothing, whatever it holds
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) x[c] = c0 + e + c > row ? 0.f : x[c];
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) w[e + c] = c0 + e + c > row ? 0.f : w[e + c];
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) sum[c >> 1 & 1] = fma2(mk2(w[e + c], w[e + c + 1]), mk2(x[c], x[c + 1]), sum[c >> 1 & 1]);
                     }
-                    nd = -row_total(own);
+                    if (j < first) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(dsfull);
+                        continue;
+                    }
+                    const u64 both = add2(sum[0], sum[1]);
+                    nd = -row_total(lo2(both) + hi2(both));
                 }
 #pragma unroll
                 for (int e = 0; e < 64; e += 32) {
@@ -722,12 +739,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) times2(x + c, w + e + c, mk2(nd, nd));
-                    if (j == 0) {
+                    if (j == first) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) x[c] = c0 + e + c > row ? 0.f : x[c];
                     }
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) off = add2(off, mk2(x[c], x[c + 1]));
 #pragma unroll
                     for (int c = 0; c < 16; ++c) z[e / 2 + c] = pack_bf2(x[2 * c], x[2 * c + 1]);
                 }
@@ -737,7 +752,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(dsfull);
             }
-            if (N > 1) nd -= row_total(lo2(off) + hi2(off));
             if (half == 0 && on) a.delta[t.h * a.T + r] = -nd;
         }
     } else {

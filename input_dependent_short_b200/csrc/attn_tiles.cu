@@ -1,4 +1,4 @@
-// The tile list of packed documents, and the backward's row sums.
+// The tile list of packed documents, the fp32 backward's row sums, and the sum of dk's and dv's parts.
 //
 // The host does not know the documents' lengths (they are offsets on the
 // device), so one block turns them into a list of tiles, sorted so that the
@@ -113,10 +113,9 @@ __global__ void __launch_bounds__(1024) k_attn_tiles(const int32_t *__restrict__
 
 // L lanes of 16 bytes cover a head; a warp takes 4 x 32 / L consecutive (row,
 // head) pairs at a time, all their loads in flight before the first sum.
-template <typename T>
-__global__ void __launch_bounds__(256) k_attn_delta(const T *__restrict__ o, const T *__restrict__ dout,
+__global__ void __launch_bounds__(256) k_attn_delta(const float *__restrict__ o, const float *__restrict__ dout,
                                                     float *__restrict__ delta, int64_t rows, int Hq, int d, int L) {
-    constexpr int V = VecOf<T>::V, U = 4;
+    constexpr int V = VecOf<float>::V, U = 4;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, per = 32 / L, sub = lane / L, pos = lane % L;
@@ -221,19 +220,13 @@ cudaError_t launch_attn_tiles(const Ctx &c, const int32_t *cu, int64_t n_docs, i
                       bytes > (size_t)100 << 20 ? 1 : 0, (int)attn_max_tiles(T, n_docs, rows), static_cast<int *>(rising), static_cast<int *>(falling));
 }
 
-cudaError_t launch_attn_delta(const Ctx &c, int dtype, int64_t T, int Hq, int d, const void *o, const void *dout,
-                              float *delta) {
-    const int V = dtype == DSC_BF16 ? 8 : 4;
+cudaError_t launch_attn_delta(const Ctx &c, int64_t T, int Hq, int d, const float *o, const float *dout, float *delta) {
     int L = 1;
-    while (L < 32 && L * V < d) L <<= 1;
+    while (L < 32 && L * VecOf<float>::V < d) L <<= 1;
     const int64_t warps = (T * Hq + 4 * (32 / L) - 1) / (4 * (32 / L));
     const int64_t want = (warps + 7) / 8, most = (int64_t)c.sms * 8;
-    const dim3 grid((unsigned)(want < most ? want : most));
-    if (dtype == DSC_BF16)
-        return launch_pdl(k_attn_delta<bf16>, grid, dim3(256), 0, c.stream, static_cast<const bf16 *>(o),
-                          static_cast<const bf16 *>(dout), delta, T, Hq, d, L);
-    return launch_pdl(k_attn_delta<float>, grid, dim3(256), 0, c.stream, static_cast<const float *>(o),
-                      static_cast<const float *>(dout), delta, T, Hq, d, L);
+    return launch_pdl(k_attn_delta, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, c.stream, o, dout, delta, T, Hq,
+                      d, L);
 }
 
 }  // namespace dsc

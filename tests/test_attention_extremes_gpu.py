@@ -208,3 +208,63 @@ def test_a_feed_whose_waits_run_out_hands_over_no_item():
     o, _ = dsc.dsc_fwd_attn_varlen(q, k, v, cu_of(docs))
     ro, bo, _, _ = ref.attn_fwd(q, k, v, docs, 0.125, BF)
     ref.check("o", o, ro, bo)
+
+
+def without_the_rounding_of_o(bound, q, k, v, do, scale):
+    """attn_ref's bound of a document's dq less what it allows for a D = do . o
+    that comes from a rounded o: D as an fp32 sum over the probabilities."""
+    n, Hq, _ = q.shape
+    u, g = ref.U[BF], Hq // k.shape[1]
+    seen = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    far = (torch.arange(n, device="cuda") >= 128).double()[:, None]
+    out = bound.clone()
+    for h in range(Hq):
+        qq, kk, vv, gg = q[:, h].double(), k[:, h // g].double(), v[:, h // g].double(), do[:, h].double()
+        _, _, p, _, eP = ref._probs(qq, kk, scale, seen)
+        mean = (p * (gg.abs() @ vv.abs().T)).sum(1, keepdim=True)
+        out[:, h] -= (1 + u) * scale * ((p * ((2 * u + eP) * mean * far)) @ kk.abs())
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("n", [129, 256, 257, 385, 700])
+def test_dq_of_rows_that_one_key_carries(n, d):
+    """The first key takes all but 2^-8 or less of every row, so dP - D is small
+    beside D: o rounds to 1 - 2^-9 +- 2^-9 and a D that came from it would be off
+    by up to 2^-9, five times the bound."""
+    Hq, Hkv, scale = 2, 1, 1 / math.sqrt(d)
+    q, k, v = (0.3 * torch.randn(n, h, d, generator=gen(190 + i), device="cuda") for i, h in enumerate((Hq, Hkv, Hkv)))
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    k[0, :, 0] = math.log(n * 2.0 ** 8) / scale
+    v[0] = 1.0
+    q, k, v = q.to(BF), k.to(BF), v.to(BF)
+    do = torch.ones(n, Hq, d, dtype=BF, device="cuda")
+    cu = cu_of([n])
+    o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu)
+    got = dsc.dsc_bwd_attn_varlen(q, k, v, o, lse, do, cu)
+    want, bound = ref.attn_bwd(q, k, v, do, [n], scale, BF)
+    bound[0] = without_the_rounding_of_o(bound[0], q, k, v, do, scale)
+    for name, g, w, b in zip(("dq", "dk", "dv"), got, want, bound):
+        ref.check(name, g, w, b)
+
+
+@pytest.mark.parametrize("docs,Hq,Hkv,d", [([700, 129, 300], 4, 2, 128), ([1500], 3, 3, 64), ([257, 640], 7, 1, 96)], ids=str)
+def test_dq_is_as_near_as_its_own_roundings_leave_it(docs, Hq, Hkv, d):
+    """Sharp rows (scores of a standard deviation of 4): dq within the bound that
+    counts the rounding of dS and of the result alone, and in the mean square no
+    further off than these two roundings, each uniform over a step (2^-8 / sqrt 3
+    relative at most)."""
+    T, scale, t0 = sum(docs), 1 / math.sqrt(d), 0
+    q, k, v = qkv(T, Hq, Hkv, d, BF, seed=200, gain=4.0)
+    do = torch.randn(T, Hq, d, generator=gen(201), device="cuda").to(BF)
+    cu = cu_of(docs)
+    o, lse = dsc.dsc_fwd_attn_varlen(q, k, v, cu)
+    dq = dsc.dsc_bwd_attn_varlen(q, k, v, o, lse, do, cu)[0]
+    want, bound = ref.attn_bwd(q, k, v, do, docs, scale, BF)
+    for n in docs:
+        r = slice(t0, t0 + n)
+        ref.check("dq", dq[r], want[0][r], without_the_rounding_of_o(bound[0][r], q[r], k[r], v[r], do[r], scale))
+        t0 += n
+    err = ((dq.double() - want[0]).norm() / want[0].norm()).item()
+    print(f"dq: {err:.5f} of its norm")
+    assert err <= math.sqrt(2) * 2.0 ** -8 / math.sqrt(3)
