@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto kraw = [&](int s) { return bars + 112u + 8u * (uint32_t)s; };
     auto vfull = [&](int s) { return bars + 136u + 8u * (uint32_t)s; };
     auto vempty = [&](int s) { return bars + 152u + 8u * (uint32_t)s; };
+    const uint32_t sumfull = bars + 168, sumread = bars + 176;
     const Feed feed(sbase, smem, S::FEED);
     float *sums = reinterpret_cast<float *>(smem + S::SUMS);
 
@@ -518,6 +519,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::mbar_init(dsfull, 8);
         tc::mbar_init(accfull, 1);
         tc::mbar_init(accempty, 4);
+        tc::mbar_init(sumfull, 8);
+        tc::mbar_init(sumread, 8);
         for (int s = 0; s < 2; ++s) tc::mbar_init(sfull(s), 1);
         for (int s = 0; s < S::KS; ++s) {
             tc::mbar_init(kfull(s), 1);
@@ -670,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane, c0 = 64 * half;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const float c2 = a.scale * LOG2E;
-        int g = 0;
+        int g = 0, totals = 0;  // steps and row totals so far
         for (int k = 0;; ++k) {
             const Item t = feed.get(k, wait, timed_out);
             feed.done(k, lane);
@@ -686,12 +689,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float nl = on ? -a.lse[t.h * a.T + r] * LOG2E : -INFINITY;
             float nd = 0.f;  // -D
             u64 sum[2] = {0, 0};  // of P dP, this half's columns
-            // Sum over the row of both halves' `own`.
+            // Sum over the row of both halves' `own`.  Bounded waits, not bar.sync: a warp whose wait has run out takes
+            // no further item, and the others must not wait for it without end.
             auto row_total = [&](float own) {
-                asm volatile("bar.sync 1, 256;" ::: "memory");  // the last item's have been read
+                if (totals) wait(sumread, (uint32_t)((totals - 1) & 1));  // the last item's have been read
+                __syncwarp();
                 sums[half * ROWS + row] = own;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                return sums[row] + sums[ROWS + row];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(sumfull);
+                wait(sumfull, (uint32_t)(totals & 1));
+                ++totals;
+                const float v = sums[row] + sums[ROWS + row];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(sumread);
+                return v;
             };
             for (int j = 0; j < M; ++j, ++g) {
                 const uint32_t tb = tS + 128u * (g & 1) + lanes + c0;
