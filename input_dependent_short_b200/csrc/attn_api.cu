@@ -98,8 +98,8 @@ int bwd_rows(const dsc_attn_problem &p) { return p.dtype == DSC_BF16 ? ATTN_TC_B
 // The tensor-core kernels make short lists themselves, where every block has
 // two items at most.  (Beyond that the items are dealt out in turn instead of
 // drawn as blocks get free, and the balance is worth more than the launch:
-// forward and backward of 5003 tokens, 14/2 heads, 152 us against 130; three
-// prompts of 300 tokens in all 14 us against 18.)
+// forward and backward of 5003 tokens, 14/2 heads, 123 us against 113; three
+// prompts of 300 tokens in all 9.6 us against 11.5, replayed from a graph.)
 bool inline_list(const dsc_attn_problem &p, int64_t n_docs, int rows) {
     const int64_t tiles = attn_max_tiles(p.T, n_docs, rows);
     return p.dtype == DSC_BF16 && tiles <= INLINE_TILES && tiles * p.Hq <= 2 * ctx(nullptr).sms;
@@ -234,7 +234,7 @@ dsc_status dsc_bwd_attn_varlen(const dsc_attn_problem *p, const int32_t *cu_seql
     } else {
         if (e == cudaSuccess)
             e = launch_attn_delta(c, p->T, a.Hq, a.d, static_cast<const float *>(o), static_cast<const float *>(dout), delta);
-        // the longer kernel first: the other's blocks fill its last SMs (187 us against 197, 1500 tokens)
+        // dk, dv first: 187 us against 197 the other way round (1500 tokens, 8/4 heads of 64)
         a.list = falling;
         if (e == cudaSuccess) e = launch_attn_dkv_simt(c, a, tiles);
         a.list = rising;

@@ -1,7 +1,8 @@
 // Attention of one new token per sequence over a paged key-value cache.
 //
-// Every key and value is read once and used for the group's query heads; the
-// time is that of reading them.  The lengths live on the device and may differ
+// A key and value is read once for a chunk of its group's query heads (16 in bf16,
+// 4 in fp32; larger groups read the cache once a chunk); the time is that of
+// reading them.  The lengths live on the device and may differ
 // a lot, so the work is dealt out there: the cache is cut into units of 64
 // tokens of one (sequence, key head, chunk of its query heads) -- a segment's
 // units are consecutive -- and block c of G takes units [c U / G, (c+1) U / G).

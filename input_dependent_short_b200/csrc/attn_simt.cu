@@ -10,9 +10,9 @@
 // 32 rows rather than 64 (with 256 threads): a training step of 1500 tokens and
 // 8 heads of 64 has too few tiles of 64 to fill the GPU and three to four
 // blocks of this size share an SM, so one's loads run under another's products.
-// Bound by FMA issue and shared memory about evenly (a 4 x 4 thread tile reads 32
-// fp32 for 64 products): 4096 tokens, 8 heads of 64, forward 524 us and gradients
-// 1626 us (33 and 26 of 72 TFLOP/s).
+// Bound by the loads from shared memory (a 4 x 4 thread tile reads 32 fp32 for 64
+// products: that pipe is 76 to 84 % busy, the FMA pipe 55 to 58 %): 4096 tokens,
+// 8 heads of 64, forward 524 us and gradients 1626 us (33 and 26 of 72 TFLOP/s).
 //
 // Operand rows outside the document are zeros, never what memory holds there,
 // and a masked probability is an exact zero that is not multiplied with

@@ -24,7 +24,7 @@
 // there back.  5 products a pair of tiles instead of 3, and no pass over o: the
 // gradients of 16384 tokens in 23 documents, 16 heads of 128, take 299 us
 // against 283 with a D from o, of one document of 8192, 32/8 heads, 1887
-// against 1471 (the added steps' K and V come from L2 at 10 TB/s, which bounds them).
+// against 1471 (the added steps' K and V come from L2 at 9 TB/s, which bounds them).
 //
 // Roles as in the forward: warps 0-7 do the elementwise part (a thread owns a
 // row of the 128 x 128 tile and 64 of its columns; P^T and dS^T go back to
@@ -61,9 +61,9 @@ struct BwdMaps {
 
 // Four probabilities 2^(S c + n) in place.  With heads of 64 the products are
 // short and the exponential unit's 16 results a cycle and SM hold a step up, so
-// every other pair goes to the FMA pipe (4096 tokens, 16 heads: 169 us against
-// 175); with 128 the exponentials run under the products (5.56 ms against 5.70
-// for 16384 tokens, 32/8 heads).
+// every other pair goes to the FMA pipe (5003 tokens, 14/2 heads: gradients 86 us
+// against 94); with 128 the exponentials run under the products (8192 tokens,
+// 32/8 heads: 1943 us against 1972 with half of them there).
 template <int DP> __device__ __forceinline__ void weights4(float *s, u64 c, u64 n0, u64 n1) {
     const u64 x = fma2(mk2(s[0], s[1]), c, n0), z = fma2(mk2(s[2], s[3]), c, n1);
     s[0] = ex2(lo2(x));

@@ -22,7 +22,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // consecutive places, the most expensive first: they read the same keys and
 // values, or queries and gradients.  (23 documents, 16 heads of 128, 268 MB:
 // by cost half of the reads missed L2 and the inputs were read 1.6 times;
-// gradients 359 -> 339 us.  7 documents, 20 MB: 87 us by cost, 92 by document.)
+// gradients 336 us by cost, 302 by document.  7 documents, 20 MB, forward and
+// gradients: 114 us by cost, 127 by document.)
 //
 // Documents that do not overlap have `cap` tiles at most.  Offsets that go back
 // and forth can ask for any number (2^23 documents of 2^30 rows: 2^48 tiles):
@@ -180,10 +181,9 @@ template <typename T, typename I> __global__ void __launch_bounds__(256) k_attn_
 // A key tile's work grows with the group, and few key heads may leave SMs idle:
 // the group's query heads are shared out to as many blocks (a divisor of the
 // group) as give three items an SM.  Each then writes fp32 parts, read once more
-// by k_attn_dkv_sum.  (5003 tokens, 14/2 heads of 64: dk and dv 149 us by one
-// block a key tile and head, 52 + 8 us shared out.  8192 tokens, 32/8 heads of
-// 128, 512 key tiles and heads: gradients 1440 us by one block each, 1500 us
-// shared out by two.)
+// by k_attn_dkv_sum.  (5003 tokens, 14/2 heads of 64: gradients 109 us by one
+// block a key tile and head, 84 us shared out.  8192 tokens, 32/8 heads of 128,
+// 512 key tiles and heads: 1922 us by one block each, 1999 us shared out by two.)
 int attn_dkv_splits(int64_t T, int rows, int Hkv, int group, int sms) {
     const int64_t items = (T + rows - 1) / rows * Hkv;
     for (int n = 1; n < group; ++n)
